@@ -264,7 +264,9 @@ def run(state):
         api.cache_write(s["k"], s["v"], s["cache"], starts=s["starts"], new_lens=lens)
         return s["cache"]
     if c["op"] == "read":
-        return api.cache_read(s["cache"], c["T"], dtype=_DT[c["dtype"]], starts=s["starts"], lens=lens)
+        B, T, Hkv, D = c["B"], c["T"], c["Hkv"], c["D"]
+        out = tuple(torch.zeros((B, T, Hkv, D), dtype=_DT[c["dtype"]], device="cuda") for _ in range(2)) if c["ragged"] else None
+        return api.cache_read(s["cache"], T, dtype=_DT[c["dtype"]], starts=s["starts"], lens=lens, out=out)
     if c["op"] == "quant":
         o, lse, _ = api.decode_quant(s["q"], s["cache"], 0.0, cache_lens=lens)
     else:
