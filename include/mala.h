@@ -395,6 +395,12 @@ size_t mala_decode_quant_workspace_size(int batch, int heads_q, int head_dim, in
  * every tile is kept, and the keys are divided evenly over about num_splits
  * CTAs a sequence and KV head instead, whatever the sequences' lengths.
  *
+ * The weight p 2^e_v of a key (e_v: its value row's exponent) enters the product
+ * with the codes with 11 bits (fp32 queries: 22), or within 2^-39 (2^-50) of
+ * the head's largest weight where that is more.  So o is accurate element by
+ * element, but for channels that are zero in all rows within 2^28 of the head's
+ * largest: there the second limit holds.
+ *
  *  q [batch, heads_q, head_dim]   q_dtype;   o [batch, heads_q, head_dim]   out_dtype
  *  k_codes, v_codes, k_exps, v_exps: a cache as above
  *  cache_lens [batch] int32, device memory, 4-byte aligned, or NULL: every

@@ -159,6 +159,7 @@ decode_quant_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     xsum[warp][2 * cq] = l0; xsum[warp][2 * cq + 1] = l1;
   }
   __syncthreads();                       // every ring is idle too: its memory takes the warps' O
+  run.join_o();
   const float f0 = run.z0 == -INFINITY ? 0.f : ex2(run.z0 - kLift - run.m0);
   const float f1 = run.z1 == -INFINITY ? 0.f : ex2(run.z1 - kLift - run.m1);
   constexpr int kPitch = D + 4;          // spreads the heads' rows over the banks

@@ -259,6 +259,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap mk, const __grid_consta
       if (i + 1 < count) at.next(a);
       if (i + 1 < count && at.b == b) continue;
 
+      run.join_o();
       float l0 = head_sum(run.l0), l1 = head_sum(run.l1);
       float r0 = kQuant ? l0 : head_sum(run.r0), r1 = kQuant ? l1 : head_sum(run.r1);
       // one head's warps agree on a reference

@@ -14,14 +14,21 @@
 //     P^T comes from S^T's accumulator by movmatrix.
 // e4m3 codes widen exactly to fp16.  q enters as fp16 after a power-of-two
 // scaling of each head's row (exact but for elements 2^-24 below the row's
-// largest); fp32 queries enter as a sum of two fp16 numbers (22 bits).
+// largest); fp32 queries enter as a sum of two fp16 numbers (22 bits, for
+// elements down to 2^-12 of the row's largest; 2^-34 of that below).
 // The key's scale multiplies its score.  The value's scale goes into the
-// exponent: w = 2^(s + e_v - z) with a running reference z of its own, so w
-// has its 11 bits wherever p times the value's size matters, and neither
-// overflows nor flushes (below 2^-38 of the largest).  fp32 queries take w as a
-// sum of two fp16 numbers as well.  l sums the unrounded p in fp32, and
-// normalises o; bf16 weights, of 8 bits, are summed as rounded for that too.
-// References move only when they would grow by more than 2^8.
+// exponent: w = 2^(s + e_v - z) with a running reference z of its own, one a
+// head.  The largest w so far is at least 2^kLift, near fp16's top, so that w has
+// fp16's 11 bits down to 2^-28 of it, and is off by at most 2^-39 of it below
+// that.  fp32 queries take w as hi + lo / kLoScale, two fp16 numbers whose
+// products gather in accumulators of their own (as a plain lo, the rest of w
+// would go under fp16's smallest step, 2^-24, while hi still has all its bits):
+// 22 bits down to 2^-28 of the largest w, 2^-50 of it below.  So what is left out is
+// small beside a head's largest p 2^e_v: in a channel where the rows of that size hold
+// zeros, rows more than 2^28 times smaller keep fewer bits than these.
+// l sums the unrounded p in fp32, and normalises o; bf16 weights, of 8 bits,
+// are summed as rounded for that too.
+// p's reference moves only when it would grow by more than 2^8, z by more than 2.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,8 +44,10 @@ using namespace tc;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4;               // warps of a CTA
-constexpr float kSlack = 8.0f;          // references move past 2^8 growth
-constexpr float kLift = 6.0f;           // w <= 2^(kSlack + kLift) < fp16's largest
+constexpr float kSlack = 8.0f;          // p's reference moves past 2^8 growth
+constexpr float kSlackW = 1.0f;         // w's past 2
+constexpr float kLift = 14.0f;          // w <= 2^(kSlackW + kLift) < fp16's largest
+constexpr float kLoScale = 2048.0f;     // what hi leaves of w, at most 2^-11 of it, times this fits where w does
 
 template <int D, bool kQuant>
 struct Layout {
@@ -208,6 +217,7 @@ struct Running {
 
   Queries<D, kQuant, kWide> q;
   float o[kOT][4];
+  float olo[kWide ? kOT : 1][4];          // the lo weights' products, kLoScale times too large
   // of this lane's heads 2cq, 2cq + 1: reference and sum of p, reference of w, and (bf16) sum of the rounded p
   float m0, m1, l0, l1, z0, z1, r0, r1;
 
@@ -217,11 +227,26 @@ struct Running {
 #pragma unroll
     for (int t = 0; t < kOT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+      for (int e = 0; e < 4; ++e) {
+        o[t][e] = 0.f;
+        if constexpr (kWide) olo[t][e] = 0.f;
+      }
   }
   __device__ __forceinline__ void scale_o(float f0, float f1) {
 #pragma unroll
-    for (int t = 0; t < kOT; ++t) { o[t][0] *= f0; o[t][1] *= f1; o[t][2] *= f0; o[t][3] *= f1; }
+    for (int t = 0; t < kOT; ++t) {
+      o[t][0] *= f0; o[t][1] *= f1; o[t][2] *= f0; o[t][3] *= f1;
+      if constexpr (kWide) { olo[t][0] *= f0; olo[t][1] *= f1; olo[t][2] *= f0; olo[t][3] *= f1; }
+    }
+  }
+  // o whole: before a record is made of it.
+  __device__ __forceinline__ void join_o() {
+    if constexpr (kWide) {
+#pragma unroll
+      for (int t = 0; t < kOT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][e] += olo[t][e] * (1.f / kLoScale);
+    }
   }
 
   // Scores of a sub-tile in log2 units, -inf from key n on: acc[mt] = keys 16mt + {gq, gq + 8} x heads {2cq, 2cq + 1}.
@@ -311,10 +336,10 @@ struct Running {
           zx0 = fmaxf(zx0, acc[mt][2 * hr] + ve[mt][hr]);
           zx1 = fmaxf(zx1, acc[mt][2 * hr + 1] + ve[mt][hr]);
         }
-      if (__any_sync(kFull, zx0 > z0 + kSlack || zx1 > z1 + kSlack)) {
+      if (__any_sync(kFull, zx0 > z0 + kSlackW || zx1 > z1 + kSlackW)) {
         zx0 = head_max(zx0);
         zx1 = head_max(zx1);
-        const float n0 = zx0 > z0 + kSlack ? zx0 : z0, n1 = zx1 > z1 + kSlack ? zx1 : z1;
+        const float n0 = zx0 > z0 + kSlackW ? zx0 : z0, n1 = zx1 > z1 + kSlackW ? zx1 : z1;
         scale_o(n0 == z0 ? 1.f : ex2(z0 - n0), n1 == z1 ? 1.f : ex2(z1 - n1));
         z0 = n0;
         z1 = n1;
@@ -335,7 +360,7 @@ struct Running {
           w.hi[mt][hr] = movmatrix(h);
           if constexpr (kWide) {
             const __half2 hh = *reinterpret_cast<const __half2*>(&h);
-            w.lo[mt][hr] = movmatrix(pack_f16(w0 - __low2float(hh), w1 - __high2float(hh)));
+            w.lo[mt][hr] = movmatrix(pack_f16((w0 - __low2float(hh)) * kLoScale, (w1 - __high2float(hh)) * kLoScale));
           }
         } else {
           const uint32_t h = pack_bf16(p0, p1);
@@ -376,10 +401,10 @@ struct Running {
           const uint32_t x2 = __byte_perm(v[2][i], v[3][i], 0x5140), y2 = __byte_perm(v[2][i], v[3][i], 0x7362);
           uint32_t a0 = e4m3x2_f16x2(x), a1 = e4m3x2_f16x2_hi(x), a2 = e4m3x2_f16x2(x2), a3 = e4m3x2_f16x2_hi(x2);
           mma16816<true>(o[2 * i], a0, a1, a2, a3, w.hi[mt][0], w.hi[mt][1]);
-          if constexpr (kWide) mma16816<true>(o[2 * i], a0, a1, a2, a3, w.lo[mt][0], w.lo[mt][1]);
+          if constexpr (kWide) mma16816<true>(olo[2 * i], a0, a1, a2, a3, w.lo[mt][0], w.lo[mt][1]);
           a0 = e4m3x2_f16x2(y); a1 = e4m3x2_f16x2_hi(y); a2 = e4m3x2_f16x2(y2); a3 = e4m3x2_f16x2_hi(y2);
           mma16816<true>(o[2 * i + 1], a0, a1, a2, a3, w.hi[mt][0], w.hi[mt][1]);
-          if constexpr (kWide) mma16816<true>(o[2 * i + 1], a0, a1, a2, a3, w.lo[mt][0], w.lo[mt][1]);
+          if constexpr (kWide) mma16816<true>(olo[2 * i + 1], a0, a1, a2, a3, w.lo[mt][0], w.lo[mt][1]);
         }
       } else {
 #pragma unroll
