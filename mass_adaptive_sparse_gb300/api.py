@@ -545,7 +545,9 @@ def _code(dtype):
 def decode_quant(q, cache, tau=1.0, *, block=128, num_splits=None, softmax_scale=None, out_dtype=None, counts=False,
                  mask=False, cache_lens=None, stream=None):
     """Decode over an 8-bit cache; returns (o, lse, info) as decode does.
-    `num_splits` None: as many as fill the GPU (16 with `counts`, which has an entry a split)."""
+    `num_splits` None: as many as fill the GPU, whether `counts` (which has an entry a split) and `mask` are asked for or
+    not.  With tau > 0 each split decides for itself which tiles it keeps: give `num_splits` where the answer must not
+    depend on the GPU, the batch, the cache's capacity and q's type."""
     if stream is not None:
         with torch.cuda.stream(stream):        # its buffers belong to the stream that the call runs on
             return decode_quant(q, cache, tau, block=block, num_splits=num_splits, softmax_scale=softmax_scale,
@@ -553,7 +555,7 @@ def decode_quant(q, cache, tau=1.0, *, block=128, num_splits=None, softmax_scale
     kc, ke, vc, ve = cache
     info = {}
     if counts:
-        num_splits = 16 if num_splits is None else num_splits
+        num_splits = _b().decode_quant_splits(q, kc, tau) if num_splits is None else num_splits
         info["counts"] = torch.zeros((kc.shape[0], kc.shape[2], num_splits), dtype=torch.int32, device=q.device)
     if mask:
         info["mask"] = torch.zeros((kc.shape[0], kc.shape[2], _ntiles(kc.shape[1], block)), dtype=torch.uint8,

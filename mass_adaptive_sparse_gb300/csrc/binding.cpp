@@ -256,6 +256,27 @@ struct Scratch {
   }
 };
 
+// The number of splits of a decode over a cache [B, N, Hkv, D] that is not given one.
+int64_t quant_splits(const Place& p, const at::Tensor& q, const at::Tensor& k_codes, double tau) {
+  const int64_t D = k_codes.size(3), tiles = (k_codes.size(1) + 127) / 128;
+  const int64_t rows = std::max<int64_t>(1, k_codes.size(0) * k_codes.size(2));
+  if (!(tau > 0)) return splits_for((D == 64 ? 4 : 2) * p.sms(), rows, tiles);
+  // Whole waves of the CTAs that the GPU holds, of about 32 tiles a CTA: each is one KV head's, and the CTAs of a
+  // row of heads drift apart over a long split (128K x 8 sequences: 337 us with 32 splits, 368 with five)
+  const int64_t slots = (D == 64 ? 4 : q.scalar_type() == at::kFloat ? 2 : 3) * static_cast<int64_t>(p.sms());
+  const int64_t waves = std::max<int64_t>(1, std::llround(static_cast<double>(rows * tiles) / (32.0 * slots)));
+  return std::max<int64_t>(1, std::min<int64_t>({256, tiles, slots * waves / rows}));
+}
+
+// (q, k_codes, tau) -> the number of splits that decode_quant takes by itself
+PyObject* decode_quant_splits(PyObject* const* a) {
+  const at::Tensor &q = tensor("q", a[0]), &kc = tensor("k_codes", a[1]);
+  if (kc.dim() != 4) throw Refused{"cache codes must be [B, N, Hkv, D]"};
+  Place p;
+  p.at(kc);
+  return PyLong_FromLongLong(quant_splits(p, q, kc, number(a[2])));
+}
+
 // (q, k_codes, k_exps, v_codes, v_exps, o, lse, workspace, cache_lens, counts, mask, block, num_splits, tau, scale,
 // out dtype, stream) -> status, o, lse; None: a new output or workspace, num_splits that fill the GPU, 1 / sqrt(D)
 PyObject* decode_quant(PyObject* const* a) {
@@ -268,21 +289,7 @@ PyObject* decode_quant(PyObject* const* a) {
   void *pq = p.at(q), *kc = p.at(c.kc), *ke = p.at(c.ke), *vc = p.at(c.vc), *ve = p.at(c.ve);
   const int64_t block = integer(a[11]);
   const double tau = number(a[13]);
-  int64_t splits;
-  if (a[12] != Py_None) {
-    splits = integer(a[12]);
-  } else {
-    const int64_t tiles = (c.N + 127) / 128, rows = std::max<int64_t>(1, c.B * c.H);
-    if (tau > 0) {
-      // Whole waves of the CTAs that the GPU holds, of about 32 tiles a CTA: each is one KV head's, and the CTAs of a
-      // row of heads drift apart over a long split (128K x 8 sequences: 337 us with 32 splits, 368 with five)
-      const int64_t slots = (c.D == 64 ? 4 : q.scalar_type() == at::kFloat ? 2 : 3) * static_cast<int64_t>(p.sms());
-      const int64_t waves = std::max<int64_t>(1, std::llround(static_cast<double>(rows * tiles) / (32.0 * slots)));
-      splits = std::max<int64_t>(1, std::min<int64_t>({256, tiles, slots * waves / rows}));
-    } else {
-      splits = splits_for((c.D == 64 ? 4 : 2) * p.sms(), rows, tiles);
-    }
-  }
+  const int64_t splits = a[12] != Py_None ? integer(a[12]) : quant_splits(p, q, c.kc, tau);
   void *counts = nullptr, *mask = nullptr;
   if (a[9] != Py_None) {
     const at::Tensor& t = tensor("retained_counts", a[9]);
@@ -402,6 +409,7 @@ PyMethodDef methods[] = {
     MALA_METHOD(cache_write, 9),
     MALA_METHOD(cache_read, 12),
     MALA_METHOD(decode_quant, 17),
+    MALA_METHOD(decode_quant_splits, 3),
     MALA_METHOD(decode_shared, 14),
     {nullptr, nullptr, 0, nullptr}};
 

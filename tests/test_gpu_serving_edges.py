@@ -111,3 +111,37 @@ def test_decode_quant_large_rows_with_empty_channels(dtype, D, tau, ratio):
     want, limit = small_weights_limit(q.double(), k.double(), v64, scale_of, 1.0, dtype)
     off = (o[0].double().cpu() - want).abs()
     assert (off <= limit).all(), f"off by {float((off / limit).max()):.3g} of the bound"
+
+
+# ---------------------------------------------------------------------------
+# What is asked for beside the answer
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tau", [0.0, 16.0])
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (FP32, 64)])
+def test_decode_quant_counts_and_mask_do_not_change_the_answer(dtype, D, tau):
+    """Without num_splits the same splits are taken, whatever is asked for beside o and lse; the counts are theirs."""
+    B, N, Hkv = 3, 7000, 8             # 19 or 25 splits of three tiles on 152 multiprocessors
+    host = ref.random_cache(B, N, Hkv, D, 17)
+    cache = cuda(host)
+    g = torch.Generator().manual_seed(23)
+    near = ref.values(*host[:2])[:, 100].float()                      # queries that lean towards one key: tiles to skip
+    near = near / near.square().mean(-1, keepdim=True).sqrt()
+    q = (torch.randn((B, 4 * Hkv, D), generator=g) + 6 * near.repeat_interleave(4, 1)).to(dtype).cuda()
+    lens = i32([N, 4999, 129])
+    calls = [api.decode_quant(q, cache, tau, cache_lens=lens, counts=c, mask=m) for c, m in
+             ((False, False), (True, False), (False, True), (True, True))]
+    assert status() == 0
+    for o, lse, _ in calls[1:]:
+        assert torch.equal(o, calls[0][0]) and torch.equal(lse, calls[0][1])
+    assert torch.equal(calls[1][2]["counts"], calls[3][2]["counts"]) and torch.equal(calls[2][2]["mask"], calls[3][2]["mask"])
+    counts, mask = calls[3][2]["counts"].cpu(), calls[3][2]["mask"].cpu()
+    splits = counts.shape[2]
+    skipped = 0
+    for b, n in enumerate(lens.tolist()):
+        T = -(-n // 128)
+        per = -(-T // splits)
+        skipped += int((mask[b, :, :T] == 0).sum())
+        for h in range(Hkv):
+            assert counts[b, h].tolist() == [int(mask[b, h, i * per:min(T, (i + 1) * per)].sum()) for i in range(splits)]
+    assert (skipped > 0) == (tau > 0)
