@@ -128,8 +128,8 @@ decode_quant_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     k_issued = min(rounds, i + S + 1);
     float tm = xmax[i & 1][0][g], lt = xl[i & 1][0][g];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) { tm = fmaxf(tm, xmax[i & 1][w][g]); lt += xl[i & 1][w][g]; }
-    // Eq. (3) for head g; the group keeps a tile that one of its heads keeps
+    for (int w = 1; w < kWarps; ++w) { tm = max_nan(tm, xmax[i & 1][w][g]); lt += xl[i & 1][w][g]; }
+    // Eq. (3) for head g; the group keeps a tile that one of its heads keeps.  A NaN score keeps its tile: the answer is NaN
     const bool keep = __any_sync(kFull, g < G && (lt == 0.f || !(tm - m_g - lg2(lt) < thr)));
     if (a.mask != nullptr && tid == 0) a.mask[(static_cast<size_t>(b) * a.Hkv + hk) * Tmax + j] = keep ? 1 : 0;
     if (!keep) continue;

@@ -109,9 +109,14 @@ __device__ __forceinline__ void sts4_zero(uint32_t addr) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" :: "r"(addr), "r"(0) : "memory");
 }
 
-__device__ __forceinline__ float head_max(float x) {         // over the eight lanes that share a head
+__device__ __forceinline__ float max_nan(float x, float y) { // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float head_max(float x) {         // over the eight lanes that share a head; NaN if one is
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
+  for (int off = 4; off < 32; off <<= 1) x = max_nan(x, __shfl_xor_sync(kFull, x, off));
   return x;
 }
 __device__ __forceinline__ float head_sum(float x) {
@@ -294,17 +299,17 @@ struct Running {
     }
   }
 
-  // This lane's share of the sub-tile's largest scores.
+  // This lane's share of the sub-tile's largest scores; NaN where one is.
   __device__ __forceinline__ static void largest(const float (&acc)[kMT][4], float& x0, float& x1) {
     x0 = x1 = -INFINITY;
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
-      x0 = fmaxf(x0, fmaxf(acc[mt][0], acc[mt][2]));
-      x1 = fmaxf(x1, fmaxf(acc[mt][1], acc[mt][3]));
+      x0 = max_nan(x0, max_nan(acc[mt][0], acc[mt][2]));
+      x1 = max_nan(x1, max_nan(acc[mt][1], acc[mt][3]));
     }
   }
 
-  // Move p's reference where the scores outgrew it.
+  // Move p's reference where the scores outgrew it (a NaN does not; it reaches l by its p).
   __device__ __forceinline__ void grow(const float (&acc)[kMT][4]) {
     float x0, x1;
     largest(acc, x0, x1);

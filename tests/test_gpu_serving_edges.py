@@ -145,3 +145,34 @@ def test_decode_quant_counts_and_mask_do_not_change_the_answer(dtype, D, tau):
         for h in range(Hkv):
             assert counts[b, h].tolist() == [int(mask[b, h, i * per:min(T, (i + 1) * per)].sum()) for i in range(splits)]
     assert (skipped > 0) == (tau > 0)
+
+
+# ---------------------------------------------------------------------------
+# The skip rule where the dense passes were tested alone
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (FP32, 64)])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_decode_quant_keeps_a_tile_with_a_nan_key(dtype, D, splits):
+    """A NaN score is not below the limit: its tile is kept and the answer is NaN, however small the tile's other scores are."""
+    B, N, Hkv = 2, 1000, 2
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn((B, N, Hkv, D), generator=g) for _ in range(2))
+    q = 3 * torch.randn((B, 4 * Hkv, D), generator=g)
+    tiles = 8
+    per = -(-tiles // splits)
+    for first in range(0, tiles, per):                                # each split's newest tile holds a key like its queries
+        last = min(N, min(tiles, first + per) * 128) - 1
+        k[:, last] = q[:, ::4]
+    q = q[:, ::4].repeat_interleave(4, 1).to(dtype)
+    k[0, 77, 1, 5] = math.nan                                         # in a tile that nothing else keeps
+    cache = api.quant_cache(B, N, Hkv, D)
+    api.cache_write(k.cuda(), v.cuda(), cache)
+    o, lse, info = api.decode_quant(q.cuda(), cache, 1.0, num_splits=splits, mask=True)
+    assert status() == 0
+    mask = info["mask"].cpu()
+    assert (mask[0, 0] == 0).any() and mask[1, 1, 0] == 0             # the same tile without a NaN is skipped
+    assert mask[0, 1, 0] == 1
+    assert torch.isnan(o[0, 4:]).all() and torch.isnan(lse[0, 4:]).all()
+    assert torch.isfinite(o[0, :4]).all() and torch.isfinite(o[1]).all()
+    assert torch.isfinite(lse[0, :4]).all() and torch.isfinite(lse[1]).all()
