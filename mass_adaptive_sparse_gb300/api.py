@@ -335,7 +335,7 @@ def mala_cache_write(k, v, k_codes, k_exps, v_codes, v_exps, *, starts=None, new
 def mala_cache_read(k_codes, k_exps, v_codes, v_exps, k, v, *, starts=None, lens=None, zero_rest=False, stream=None):
     """Write the values of an 8-bit cache's rows starts[b] .. to rows 0 .. of k, v
     [B, T, Hkv, D]; rows behind lens[b] stay as they are, or become zeros."""
-    code, _, _ = _b().cache_read(k_codes, k_exps, v_codes, v_exps, k, v, 0, 0, starts, lens, int(zero_rest), _raw(stream))
+    code, _, _ = _b().cache_read(k_codes, k_exps, v_codes, v_exps, k, v, -1, -1, starts, lens, int(zero_rest), _raw(stream))
     if code:
         _check("mala_cache_read", code)
 
@@ -520,15 +520,18 @@ def cache_write(k, v, cache, *, starts=None, new_lens=None, stream=None):
     mala_cache_write(k, v, *cache, starts=starts, new_lens=new_lens, stream=stream)
 
 
-def cache_read(cache, T, *, dtype=torch.bfloat16, starts=None, lens=None, out=None, stream=None):
-    """(k, v) [B, T, Hkv, D]: the values of cache rows starts[b] + t, t < lens[b].
-    Rows behind lens[b] keep what `out` holds (without `out`: zeros)."""
+def cache_read(cache, T, *, dtype=None, starts=None, lens=None, out=None, stream=None):
+    """(k, v) [B, T, Hkv, D] of `dtype` (None: bf16, or that of `out`): the values of cache rows starts[b] + t,
+    t < lens[b].  Rows behind lens[b] keep what `out` holds (without `out`: zeros); `out` of another T or dtype than
+    these is refused."""
     if stream is not None:
         with torch.cuda.stream(stream):        # its buffers belong to the stream that the call runs on
             return cache_read(cache, T, dtype=dtype, starts=starts, lens=lens, out=out)
     kc, ke, vc, ve = cache
     k, v = (None, None) if out is None else out
-    code, k, v = _b().cache_read(kc, ke, vc, ve, k, v, T, _code(dtype), starts, lens, out is None, None)
+    if T < 0:
+        raise ValueError(f"T must not be negative, got {T}")
+    code, k, v = _b().cache_read(kc, ke, vc, ve, k, v, T, -1 if dtype is None else _code(dtype), starts, lens, out is None, None)
     if code:
         _check("mala_cache_read", code)
     return k, v

@@ -184,24 +184,29 @@ PyObject* cache_write(PyObject* const* a) {
 }
 
 // (k_codes, k_exps, v_codes, v_exps, k, v, T, dtype, starts, lens, zero_rest, stream) -> status, k, v; k = None:
-// new [B, T, Hkv, D] tensors of the dtype code
+// new [B, T, Hkv, D] tensors of the dtype code (negative: bf16); else k and v are such tensors (a negative T or dtype:
+// of any)
 PyObject* cache_read(PyObject* const* a) {
   const Cache c(a);
-  Place p;
-  void *kc = p.at(c.kc), *ke = p.at(c.ke), *vc = p.at(c.vc), *ve = p.at(c.ve);
+  const bool given = a[4] != Py_None;
+  int64_t T = integer(a[6]);
+  const int64_t code = integer(a[7]);
   at::Tensor k, v;
-  int64_t T;
-  if (a[4] == Py_None) {
-    T = integer(a[6]);
-    if (T < 0) throw Refused{"T must not be negative"};
-    k = p.empty({c.B, T, c.H, c.D}, type_of(integer(a[7])));
-    v = p.empty({c.B, T, c.H, c.D}, k.scalar_type());
-  } else {
+  if (given) {
     k = tensor("k", a[4]);
     v = tensor("v", a[5]);
-    T = k.dim() == 4 ? k.size(1) : -1;
-    want_float("k", k, {c.B, T, c.H, c.D});
+    if (T < 0) T = k.dim() == 4 ? k.size(1) : -1;
+    if (code < 0) want_float("k", k, {c.B, T, c.H, c.D});
+    else want("k", k, type_of(code), {c.B, T, c.H, c.D});
     want("v", v, k.scalar_type(), {c.B, T, c.H, c.D});
+  } else if (T < 0) {
+    throw Refused{"T must not be negative"};
+  }
+  Place p;
+  void *kc = p.at(c.kc), *ke = p.at(c.ke), *vc = p.at(c.vc), *ve = p.at(c.ve);
+  if (!given) {
+    k = p.empty({c.B, T, c.H, c.D}, code < 0 ? at::kBFloat16 : type_of(code));
+    v = p.empty({c.B, T, c.H, c.D}, k.scalar_type());
   }
   const int32_t *starts = int32s(p, "starts", a[8], c.B), *lens = int32s(p, "lens", a[9], c.B);
   void *pk = p.at(k), *pv = p.at(v), *stream = p.stream(a[11]);

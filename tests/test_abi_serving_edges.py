@@ -1,0 +1,28 @@
+"""Host-side refusals of the serving entry points that depend on more than one
+argument.  Nothing here reaches a GPU."""
+import pytest
+import torch
+
+from mass_adaptive_sparse_gb300 import api
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def test_cache_read_refuses_outputs_of_another_length_or_type():
+    """`out` is of the T and the dtype that the call names, or the call is refused; nothing of it is ignored."""
+    cache = api.quant_cache(2, 10, 2, 64, device="cpu")
+    out = tuple(torch.zeros((2, 5, 2, 64), dtype=FP32) for _ in range(2))
+    for T, dtype in ((10, FP32), (4, None), (0, None), (5, BF16)):
+        with pytest.raises(ValueError, match="k must be"):
+            api.cache_read(cache, T, dtype=dtype, out=out)
+    for T in (-1, -5):
+        with pytest.raises(ValueError, match="negative"):
+            api.cache_read(cache, T, out=out)
+        with pytest.raises(ValueError, match="negative"):
+            api.cache_read(cache, T)
+    with pytest.raises(ValueError, match="v must be"):
+        api.cache_read(cache, 5, out=(out[0], out[1][:, :4].contiguous()))
+    # the right ones go on to the check of their device, with or without the type
+    for dtype in (FP32, None):
+        with pytest.raises(ValueError, match="CUDA"):
+            api.cache_read(cache, 5, dtype=dtype, out=out)
