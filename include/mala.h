@@ -385,7 +385,8 @@ mala_status mala_cache_read(const void* k_codes, const uint8_t* k_exps, const vo
                             const int32_t* lens, int batch, int len, int cache_len, int heads_kv,
                             int head_dim, mala_dtype out_dtype, int zero_rest, void* stream);
 
-/* Bytes of device workspace mala_decode_quant needs for these sizes. */
+/* Bytes of device workspace mala_decode_quant needs for these sizes, whatever
+ * tau; 0 where num_splits is outside [1, 256] (the call refuses it). */
 size_t mala_decode_quant_workspace_size(int batch, int heads_q, int head_dim, int num_splits);
 
 /*
@@ -421,7 +422,8 @@ mala_status mala_decode_quant(const void* q, const void* k_codes, const uint8_t*
                               void* workspace, size_t workspace_bytes, int32_t* retained_counts,
                               uint8_t* tile_mask, void* stream);
 
-/* Bytes of device workspace mala_decode_shared needs for these sizes. */
+/* Bytes of device workspace mala_decode_shared needs for these sizes; 0 where
+ * a number of splits is outside [1, 256] (the call refuses it). */
 size_t mala_decode_shared_workspace_size(int batch, int heads_q, int head_dim, int prefix_splits,
                                          int suffix_splits);
 

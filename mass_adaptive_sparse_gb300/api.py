@@ -559,7 +559,8 @@ def decode_quant(q, cache, tau=1.0, *, block=128, num_splits=None, softmax_scale
     info = {}
     if counts:
         num_splits = _b().decode_quant_splits(q, kc, tau) if num_splits is None else num_splits
-        info["counts"] = torch.zeros((kc.shape[0], kc.shape[2], num_splits), dtype=torch.int32, device=q.device)
+        if 1 <= num_splits <= 256:             # the library refuses the others
+            info["counts"] = torch.zeros((kc.shape[0], kc.shape[2], num_splits), dtype=torch.int32, device=q.device)
     if mask:
         info["mask"] = torch.zeros((kc.shape[0], kc.shape[2], _ntiles(kc.shape[1], block)), dtype=torch.uint8,
                                    device=q.device)

@@ -486,7 +486,7 @@ mala_status mala_cache_read(const void* k_codes, const uint8_t* k_exps, const vo
 
 // Dense: at most four workers a split and sequence, and one record more a sequence for the cuts inside a worker.
 size_t mala_decode_quant_workspace_size(int batch, int heads_q, int head_dim, int num_splits) {
-  if (num_splits < 1) return 0;
+  if (num_splits < 1 || num_splits > 256) return 0;
   return mala_decode_workspace_size(batch, heads_q, head_dim, 4 * num_splits + 1);
 }
 
@@ -534,7 +534,7 @@ mala_status mala_decode_quant(const void* q, const void* k_codes, const uint8_t*
 
 size_t mala_decode_shared_workspace_size(int batch, int heads_q, int head_dim, int prefix_splits,
                                          int suffix_splits) {
-  if (prefix_splits < 1 || suffix_splits < 1) return 0;
+  if (prefix_splits < 1 || prefix_splits > 256 || suffix_splits < 1 || suffix_splits > 256) return 0;
   return mala_decode_workspace_size(batch, heads_q, head_dim, prefix_splits + 4 * suffix_splits + 1);
 }
 

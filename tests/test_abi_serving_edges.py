@@ -26,3 +26,14 @@ def test_cache_read_refuses_outputs_of_another_length_or_type():
     for dtype in (FP32, None):
         with pytest.raises(ValueError, match="CUDA"):
             api.cache_read(cache, 5, dtype=dtype, out=out)
+
+
+@pytest.mark.parametrize("splits", [257, 10 ** 6, 2 ** 29, 2 ** 31 - 1, -2 ** 31])
+def test_workspace_sizes_are_zero_for_splits_that_the_calls_refuse(splits):
+    """Nothing is allocated for them (and nothing overflows on the way)."""
+    lib = api.lib()
+    assert lib.mala_decode_quant_workspace_size(4, 8, 128, splits) == 0
+    assert lib.mala_decode_shared_workspace_size(4, 8, 128, splits, 2) == 0
+    assert lib.mala_decode_shared_workspace_size(4, 8, 128, 3, splits) == 0
+    assert lib.mala_decode_quant_workspace_size(4, 8, 128, 256) >= 1025 * 4 * 8 * 132 * 4
+    assert lib.mala_decode_shared_workspace_size(4, 8, 128, 256, 256) >= 1281 * 4 * 8 * 132 * 4

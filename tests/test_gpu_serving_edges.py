@@ -176,3 +176,21 @@ def test_decode_quant_keeps_a_tile_with_a_nan_key(dtype, D, splits):
     assert torch.isnan(o[0, 4:]).all() and torch.isnan(lse[0, 4:]).all()
     assert torch.isfinite(o[0, :4]).all() and torch.isfinite(o[1]).all()
     assert torch.isfinite(lse[0, :4]).all() and torch.isfinite(lse[1]).all()
+
+
+# ---------------------------------------------------------------------------
+# Refusals that no allocation comes before
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("splits", [257, 10 ** 8, -10 ** 8])
+def test_split_counts_out_of_range_are_refused_by_the_library(splits):
+    cache = api.quant_cache(2, 16, 2, 64)
+    q = torch.zeros((2, 8, 64), dtype=BF16, device="cuda")
+    p = torch.zeros((5, 2, 64), dtype=BF16, device="cuda")
+    for call in (lambda: api.decode_quant(q, cache, 0.0, num_splits=splits),
+                 lambda: api.decode_quant(q, cache, 1.0, num_splits=splits, counts=True, mask=True),
+                 lambda: api.decode_shared(q, p, p, prefix_splits=splits),
+                 lambda: api.decode_shared(q, p, p, suffix_splits=splits)):
+        with pytest.raises(api.MalaError) as err:
+            call()
+        assert err.value.code == 1
