@@ -271,9 +271,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const uint32_t colS = s * 128, colO = kColO + s * 128;
     float m = -INFINITY, l = 0.f, lr = 0.f;
     bool ok = true;
+    // After a timed-out wait the loop runs on (waits then fail at once): the lanes of a warp may see the end of a wait
+    // differently, and the loads from tensor memory take all of them.
     for (int u = 0; u < steps; ++u) {
       ok = mbar_wait(smem_u32(&bars.s_full[s]), u & 1, abortp, a.status) && ok;
-      if (!ok) break;
       fence_after_sync();
       if (work) {
         const int last = a.N - 1 - (t0 + (alone ? 2 * u + s : u)) * kBlk;      // last column with a key

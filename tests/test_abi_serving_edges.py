@@ -1,5 +1,8 @@
 """Host-side refusals of the serving entry points that depend on more than one
 argument.  Nothing here reaches a GPU."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -37,3 +40,14 @@ def test_workspace_sizes_are_zero_for_splits_that_the_calls_refuse(splits):
     assert lib.mala_decode_shared_workspace_size(4, 8, 128, 3, splits) == 0
     assert lib.mala_decode_quant_workspace_size(4, 8, 128, 256) >= 1025 * 4 * 8 * 132 * 4
     assert lib.mala_decode_shared_workspace_size(4, 8, 128, 256, 256) >= 1281 * 4 * 8 * 132 * 4
+
+
+def test_prefix_softmax_warps_stay_together_after_an_expired_wait():
+    """A wait that expires or is aborted can end differently for the lanes of a warp, and the loads from tensor memory
+    behind it need every lane.  No call can bring this about at will, so the source is read: nothing in the softmax
+    role's loop leaves it."""
+    src = open(os.path.join(os.path.dirname(api.__file__), "csrc", "prefix_tc.cu")).read()
+    role = src[src.index("softmax: thread r of slot s"):]
+    loop = role[role.index("for (int u = 0; u < steps; ++u)"):role.index("if (steps > 0)")]
+    assert "tmem_ld64_sync" in loop and "mbar_arrive(smem_u32(&bars.p_ready[s]))" in loop
+    assert not re.search(r"\b(break|continue|return|goto)\b", loop)
