@@ -6,13 +6,15 @@ import math
 import pytest
 import torch
 
+import oracle as orc
 from mass_adaptive_sparse_gb300 import api
+from tests import parity
 from tests import serving_ref as ref
 
 pytestmark = pytest.mark.gpu
 
 BF16, FP32 = torch.bfloat16, torch.float32
-KEEP_ALL = 1e-30           # a tau > 0 that skips no tile of these inputs
+KEEP_ALL = 1e-30           # a tau > 0 that skips no tile whose scores lie within 69 nats of the largest
 
 
 def i32(x):
@@ -194,3 +196,144 @@ def test_split_counts_out_of_range_are_refused_by_the_library(splits):
         with pytest.raises(api.MalaError) as err:
             call()
         assert err.value.code == 1
+
+
+TAUS = [0.0, KEEP_ALL, 16.0]
+U_W = {BF16: 2.0 ** -11, FP32: 2.0 ** -21}                # of the weights, as in the dense tests
+
+
+def leaning_queries(B, Hq, D, dtype, seed, k, at, amp=6.0):
+    """Queries that lean towards key at[b] of sequence b (k [B, N, Hkv, D], float64)."""
+    g = torch.Generator().manual_seed(seed)
+    near = torch.stack([k[b, at[b]] for b in range(B)]).float()
+    near = near / near.square().mean(-1, keepdim=True).sqrt()
+    return (torch.randn((B, Hq, D), generator=g) + amp * near.repeat_interleave(Hq // k.shape[2], 1)).to(dtype)
+
+
+def check_kept(o, lse, info, q, k, v, lens, splits, tau, rows=None):
+    """Decisions as the oracle's (borderline tiles replayed), counts of every head and split, and o and lse element by
+    element against the 64-bit softmax over the keys of the kept tiles.  Returns the number of skipped tiles."""
+    D, Hkv, dtype = q.shape[2], k.shape[2], q.dtype
+    G, scale, block = q.shape[1] // Hkv, 1 / math.sqrt(D), 128
+    mask, counts = info["mask"].cpu(), info["counts"].cpu()
+    skipped = 0
+    for b in range(q.shape[0]) if rows is None else rows:
+        n = lens[b]
+        T = -(-n // block)
+        per = -(-T // splits)
+        assert not mask[b, :, T:].any()
+        for h in range(Hkv):
+            kept = mask[b, h, :T] != 0
+            assert counts[b, h].tolist() == [int(kept[min(T, i * per):min(T, (i + 1) * per)].sum()) for i in range(splits)]
+            qh, kh, vh = q[b, h * G:(h + 1) * G].double(), k[b, :n, h], v[b, :n, h]
+            want = orc.mala_decode(qh.numpy(), kh.numpy(), vh.numpy(), scale, tau, block, splits)
+            parity.decode_expected(kept.numpy(), want.o, want.lse, want.retained, qh.numpy(), kh.numpy(), vh.numpy(), scale, tau,
+                                   block, splits)
+            skipped += int((~kept).sum())
+            keys = kept.repeat_interleave(block)[:n]
+            eo, el, absv, qk = ref.attend(qh, kh[keys], vh[keys], scale)
+            lo, ll = ref.bounds(eo, el, absv, qk, int(keys.sum()), D, U_W[dtype], ref.U[o.dtype])
+            heads = slice(h * G, (h + 1) * G)
+            assert ((o[b, heads].double().cpu() - eo).abs() <= lo).all(), f"o, b={b}, h={h}"
+            assert ((lse[b, heads].double().cpu() - el).abs() <= ll).all(), f"lse, b={b}, h={h}"
+    return skipped
+
+
+@pytest.mark.parametrize("tau", TAUS)
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (FP32, 64), (BF16, 64), (FP32, 128)])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_decode_quant_stale_rows(dtype, D, splits, tau):
+    """Rows behind the lengths hold NaN codes and the largest scales, also in tiles that a length ends in."""
+    lens = [1, 31, 33, 128, 129, 900, 1023, 1100]
+    B, N, Hkv, Hq = len(lens), 1100, 2, 8
+    cache = ref.random_cache(B, N, Hkv, D, 121)
+    k, v = (ref.values(*cache[i:i + 2]) for i in (0, 2))
+    q = leaning_queries(B, Hq, D, dtype, 14, k, [n - 1 for n in lens])
+    for b, n in enumerate(lens):
+        for i in (0, 2):
+            cache[i].view(torch.uint8)[b, n:] = 0x7f
+            cache[i + 1][b, :, n:] = 255 if b % 2 else 254
+    o, lse, info = api.decode_quant(q.cuda(), cuda(cache), tau, num_splits=splits, cache_lens=i32(lens), counts=True, mask=True)
+    assert status() == 0
+    skipped = check_kept(o, lse, info, q, k, v, lens, splits, tau)
+    assert skipped == 0 if tau == 0 else skipped > 0 or tau == KEEP_ALL
+
+
+@pytest.mark.parametrize("tau", TAUS)
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (FP32, 64)])
+def test_decode_quant_wrong_lengths_at_every_tau(dtype, D, tau):
+    """A refused length gives NaN, no kept tile and the status bit; the sequences beside it are answered."""
+    lens, N = [500, 0, 700, -3, 701, 1], 700
+    B, Hkv, Hq, splits = len(lens), 2, 8, 2
+    cache = ref.random_cache(B, N, Hkv, D, 12)
+    k, v = (ref.values(*cache[i:i + 2]) for i in (0, 2))
+    good = [b for b, n in enumerate(lens) if 1 <= n <= N]
+    q = leaning_queries(B, Hq, D, dtype, 15, k, [n - 1 if b in good else 0 for b, n in enumerate(lens)])
+    o, lse, info = api.decode_quant(q.cuda(), cuda(cache), tau, num_splits=splits, cache_lens=i32(lens), counts=True, mask=True)
+    assert status() == 2
+    for b in range(B):
+        if b not in good:
+            assert torch.isnan(o[b]).all() and torch.isnan(lse[b]).all()
+            assert not info["counts"][b].any() and not info["mask"][b].any()
+    check_kept(o, lse, info, q, k, v, lens, splits, tau, rows=good)
+
+
+@pytest.mark.parametrize("tau", TAUS)
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_decode_quant_nonfinite_rows_and_queries(dtype, tau):
+    """A NaN key makes its KV head's answers NaN, an infinite value row those that weigh it, a NaN query its own head's."""
+    B, N, Hkv, Hq, D = 3, 700, 2, 8, 128
+    g = torch.Generator().manual_seed(33)
+    k, v = (torch.randn((B, N, Hkv, D), generator=g) for _ in range(2))
+    q = torch.randn((B, Hq, D), generator=g).to(dtype)
+    k[0, 77, 1, 5] = math.nan
+    v[1, N - 1, 0, 9] = -math.inf                      # in the newest tile, which is always kept
+    q[2, 3, 0] = math.nan
+    cache = api.quant_cache(B, N, Hkv, D)
+    api.cache_write(k.cuda(), v.cuda(), cache)
+    o, lse, _ = api.decode_quant(q.cuda(), cache, tau, num_splits=1)
+    assert status() == 0
+    bad_o = torch.zeros((B, Hq), dtype=torch.bool)
+    bad_o[0, 4:] = bad_o[1, :4] = bad_o[2, 3] = True
+    bad_lse = bad_o.clone()
+    bad_lse[1] = False                                 # values do not enter it
+    assert torch.equal(torch.isnan(o).all(-1).cpu(), bad_o) and torch.equal(torch.isnan(o).any(-1).cpu(), bad_o)
+    assert torch.equal(torch.isnan(lse).cpu(), bad_lse)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (FP32, 64)])
+def test_decode_quant_same_bits_under_the_skip_rule(dtype, D):
+    cache = ref.random_cache(3, 3000, 4, D, 181)
+    q = leaning_queries(3, 16, D, dtype, 3, ref.values(*cache[:2]), [2999, 10, 1500]).cuda()
+    cache = cuda(cache)
+    a, b = (api.decode_quant(q, cache, 16.0, num_splits=3, cache_lens=i32([3000, 2999, 130]), counts=True, mask=True) for _ in range(2))
+    assert status() == 0
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert all(torch.equal(a[2][n], b[2][n]) for n in ("counts", "mask"))
+
+
+@pytest.mark.parametrize("tau", [KEEP_ALL, 1.0])
+def test_skip_rule_offsets_past_32_bits(tau):
+    """A cache whose last rows lie more than 2^31 bytes in, under the skip rule: decisions are not replayed here, but o and lse
+    are the softmax over the keys of the tiles that the mask names, the newest among them."""
+    N, Hkv, D, splits = 2_200_000, 8, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    codes = [torch.empty((1, N, Hkv, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+    exps = [torch.full((1, Hkv, N), 122, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for c in codes:
+        for i in range(0, N, 200_000):
+            c[:, i:i + 200_000] = torch.randn((1, min(200_000, N - i), Hkv, D), generator=g, device="cuda").mul_(32).to(torch.float8_e4m3fn)
+    q = torch.randn((1, 16, D), generator=g, device="cuda").to(BF16)
+    q[:, 14:] += 6 * codes[0][:, N - 1, 7:8].to(torch.float32).sign().to(BF16)   # the last head's queries lean towards the last row
+    o, lse, info = api.decode_quant(q, (codes[0], exps[0], codes[1], exps[1]), tau, num_splits=splits, counts=True, mask=True)
+    assert status() == 0
+    kept = info["mask"][0, 7] != 0
+    T = kept.numel()
+    per = -(-T // splits)
+    assert info["counts"][0, 7].tolist() == [int(kept[i * per:(i + 1) * per].sum()) for i in range(splits)]
+    assert bool(kept[-1]) and bool(kept.all()) == (tau == KEEP_ALL)
+    keys = kept.repeat_interleave(128)[:N]
+    rows = [(codes[i][0, :, 7][keys].double() * torch.exp2(exps[i][0, 7][keys].double() - 127)[:, None]) for i in (0, 1)]
+    want_o, want_lse, absv, qk = ref.attend(q[0, 14:].double(), rows[0], rows[1], 1 / math.sqrt(D))
+    lo, ll = ref.bounds(want_o, want_lse, absv, qk, int(keys.sum()), D, U_W[BF16], ref.U[BF16])
+    assert ((o[0, 14:].double() - want_o).abs() <= lo).all() and ((lse[0, 14:].double() - want_lse).abs() <= ll).all()
