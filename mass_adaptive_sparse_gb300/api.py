@@ -348,7 +348,7 @@ def mala_decode_quant(q, k_codes, k_exps, v_codes, v_exps, o, lse, workspace, *,
                       num_splits=16, tau=1.0, softmax_scale=None, retained_counts=None, tile_mask=None, stream=None):
     """mala_decode over an 8-bit cache (mala_decode_varlen with cache_lens)."""
     code, _, _ = _b().decode_quant(q, k_codes, k_exps, v_codes, v_exps, o, lse, workspace, cache_lens, retained_counts,
-                                   tile_mask, block, num_splits, tau, softmax_scale, 0, _raw(stream))
+                                   tile_mask, block, num_splits, tau, softmax_scale, -2, _raw(stream))
     if code:
         _check("mala_decode_quant", code)
 
@@ -362,7 +362,7 @@ def mala_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, o, lse, workspac
     """Exact decode of a batch behind one prefix [P, Hkv, D]; k_cache, v_cache
     [B, N, Hkv, D] hold the sequences' own rows (None: no sequence has any)."""
     code, _, _ = _b().decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, o, lse, workspace, suffix_lens,
-                                    prefix_splits, suffix_splits, softmax_scale, 0, _raw(stream))
+                                    prefix_splits, suffix_splits, softmax_scale, -2, _raw(stream))
     if code:
         _check("mala_decode_shared", code)
 

@@ -200,7 +200,7 @@ PyObject* cache_read(PyObject* const* a) {
     else want("k", k, type_of(code), {c.B, T, c.H, c.D});
     want("v", v, k.scalar_type(), {c.B, T, c.H, c.D});
   } else if (T < 0) {
-    throw Refused{"T must not be negative"};
+    throw Refused{"k must be a tensor"};
   }
   Place p;
   void *kc = p.at(c.kc), *ke = p.at(c.ke), *vc = p.at(c.vc), *ve = p.at(c.ve);
@@ -224,16 +224,19 @@ int64_t splits_for(int64_t ctas, int64_t per_split, int64_t tiles) {
   return std::max<int64_t>(1, std::min<int64_t>({256, tiles, (ctas + per_split - 1) / per_split}));
 }
 
-// Given output, or a new one of a dtype code (negative: q's type).
+// The dtype code of a call that makes no outputs of its own: None is refused for them.
+constexpr int64_t kGivenOutputs = -2;
+
+// Given output, or a new one of a dtype code (-1: q's type).
 at::Tensor output(Place& p, const char* name, PyObject* o, Shape shape, int64_t code, const at::Tensor& q) {
-  if (o == Py_None) return p.empty(shape, code < 0 ? q.scalar_type() : type_of(code));
+  if (o == Py_None && code != kGivenOutputs) return p.empty(shape, code < 0 ? q.scalar_type() : type_of(code));
   const at::Tensor& t = tensor(name, o);
   want_float(name, t, shape);
   return t;
 }
 
-at::Tensor logs(Place& p, PyObject* o, Shape shape) {
-  if (o == Py_None) return p.empty(shape, at::kFloat);
+at::Tensor logs(Place& p, PyObject* o, Shape shape, int64_t code) {
+  if (o == Py_None && code != kGivenOutputs) return p.empty(shape, at::kFloat);
   const at::Tensor& t = tensor("lse", o);
   want("lse", t, at::kFloat, shape);
   return t;
@@ -283,7 +286,8 @@ PyObject* decode_quant_splits(PyObject* const* a) {
 }
 
 // (q, k_codes, k_exps, v_codes, v_exps, o, lse, workspace, cache_lens, counts, mask, block, num_splits, tau, scale,
-// out dtype, stream) -> status, o, lse; None: a new output or workspace, num_splits that fill the GPU, 1 / sqrt(D)
+// out dtype, stream) -> status, o, lse; None: a new output (unless the dtype is kGivenOutputs) or workspace, num_splits that
+// fill the GPU, 1 / sqrt(D)
 PyObject* decode_quant(PyObject* const* a) {
   const Cache c(a + 1);
   const at::Tensor& q = tensor("q", a[0]);
@@ -306,7 +310,7 @@ PyObject* decode_quant(PyObject* const* a) {
     want("tile_mask", t, at::kByte, {c.B, c.H, block > 0 ? (c.N + block - 1) / block : 0});
     mask = p.at(t);
   }
-  const at::Tensor o = output(p, "o", a[5], {c.B, Hq, c.D}, integer(a[15]), q), lse = logs(p, a[6], {c.B, Hq});
+  const at::Tensor o = output(p, "o", a[5], {c.B, Hq, c.D}, integer(a[15]), q), lse = logs(p, a[6], {c.B, Hq}, integer(a[15]));
   const int B = as_int("B", c.B), N = as_int("N", c.N), hq = as_int("Hq", Hq), H = as_int("Hkv", c.H), D = as_int("D", c.D);
   const int blk = as_int("block", block), sp = as_int("num_splits", splits);
   void *po = p.at(o), *pl = p.at(lse), *stream = p.stream(a[16]);
@@ -349,7 +353,7 @@ PyObject* decode_shared(PyObject* const* a) {
                                      : mala::SharedPlan(p.sms(), static_cast<int>(B), static_cast<int>(P), static_cast<int>(N), lens != nullptr,
                                                         static_cast<int>(Hq), static_cast<int>(H)).best_splits();
   const int64_t ss = a[10] != Py_None ? integer(a[10]) : !sized ? 1 : splits_for((D == 64 ? 4 : 2) * p.sms(), B * H, std::max<int64_t>(1, (N + 63) / 64));
-  const at::Tensor o = output(p, "o", a[5], {B, Hq, D}, integer(a[12]), q), lse = logs(p, a[6], {B, Hq});
+  const at::Tensor o = output(p, "o", a[5], {B, Hq, D}, integer(a[12]), q), lse = logs(p, a[6], {B, Hq}, integer(a[12]));
   const int b = as_int("B", B), pl = as_int("P", P), n = as_int("N", N), hq = as_int("Hq", Hq), h = as_int("Hkv", H), d = as_int("D", D);
   const int psi = as_int("prefix_splits", ps), ssi = as_int("suffix_splits", ss);
   void *po = p.at(o), *plse = p.at(lse), *stream = p.stream(a[13]);

@@ -337,3 +337,20 @@ def test_skip_rule_offsets_past_32_bits(tau):
     want_o, want_lse, absv, qk = ref.attend(q[0, 14:].double(), rows[0], rows[1], 1 / math.sqrt(D))
     lo, ll = ref.bounds(want_o, want_lse, absv, qk, int(keys.sum()), D, U_W[BF16], ref.U[BF16])
     assert ((o[0, 14:].double() - want_o).abs() <= lo).all() and ((lse[0, 14:].double() - want_lse).abs() <= ll).all()
+
+
+def test_raw_calls_refuse_missing_outputs():
+    """The entry points that return nothing take their outputs from the caller: None is not a place to drop a result."""
+    cache = api.quant_cache(2, 16, 2, 64)
+    q = torch.zeros((2, 8, 64), dtype=BF16, device="cuda")
+    p = torch.zeros((5, 2, 64), dtype=BF16, device="cuda")
+    lse = torch.zeros((2, 8), device="cuda")
+    launched = api.mala_launch_count()
+    for o, l, name in ((None, lse, "o"), (q.clone(), None, "lse"), (None, None, "o")):
+        with pytest.raises(ValueError, match=f"{name} must be a tensor"):
+            api.mala_decode_quant(q, *cache, o, l, None)
+        with pytest.raises(ValueError, match=f"{name} must be a tensor"):
+            api.mala_decode_shared(q, p, p, None, None, o, l, None)
+    with pytest.raises(ValueError, match="k must be a tensor"):
+        api.mala_cache_read(*cache, None, None)
+    assert api.mala_launch_count() == launched
