@@ -7,8 +7,9 @@
 // each, and skips a tile whose largest score, for every query head of the KV
 // head's group, stays below m + log l + log(tau / L).  A skipped tile loads no V.
 //
-// Bound: HBM, 129 bytes a key and KV head, as much again for a kept tile.  8
-// sequences of 128K keys at tau = 1, 35 splits: 325 us, 6.7 TB/s (dense: 304).
+// Bound: HBM, D + 2 bytes a key and KV head (the value's exponent comes with the
+// key's), D more in a kept tile.  8 sequences of 128K keys at tau = 1, 35
+// splits, every tile kept: 325 us, 6.7 TB/s (dense: 304).
 //
 // One CTA of four warps per (KV head, split, sequence), a warp owns 32 keys of
 // every tile.  One barrier a tile exchanges the warps' maxima and sums; every

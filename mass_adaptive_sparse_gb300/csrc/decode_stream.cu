@@ -7,7 +7,8 @@
 // attention does not need a quadratic matrix", Method/Mechanism).
 //
 // Bound: HBM.  A key and its value are read once for the G <= 8 query heads of
-// their KV head, 2 to 4 G flops a byte.
+// their KV head: 4 D G flops over 4 D bytes of bf16 (G flops a byte) or 2 (D + 1)
+// of the 8-bit cache (about 2 G).
 //
 // Every tile is kept, so the work can be cut anywhere.  The sequences' keys, in
 // units of a sub-tile (32 keys of e4m3, 16 of bf16), are laid end to end and

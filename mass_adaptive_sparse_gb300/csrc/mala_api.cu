@@ -513,7 +513,7 @@ mala_status mala_decode_quant(const void* q, const void* k_codes, const uint8_t*
   a.lens = cache_lens;
   a.B = batch; a.N = cache_len; a.Hq = heads_q; a.Hkv = heads_kv; a.D = head_dim;
   a.q_dt = q_dtype; a.out_dt = out_dtype; a.splits = num_splits; a.min_len = 1;
-  a.tau = tau; a.log2_tau = tau > 0.f ? std::log2(tau) : 0.f;
+  a.log2_tau = tau > 0.f ? std::log2(tau) : 0.f;
   a.scale_log2 = softmax_scale * kLog2e;
   a.partial = static_cast<float*>(workspace);
   a.counts = retained_counts; a.mask = tile_mask; a.status = status;

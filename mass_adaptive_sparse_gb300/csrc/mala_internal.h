@@ -123,7 +123,7 @@ struct StreamArgs {
   int B, N, Hq, Hkv, D;
   int q_dt, out_dt, splits;
   int min_len;              // smallest legal length
-  float tau, log2_tau, scale_log2;
+  float log2_tau, scale_log2;
   // records that every (sequence, head) has, [records][B][Hq][D + 4], laid out as in DecArgs
   float* partial;
   int records;

@@ -7,7 +7,7 @@
 // the merge joins with each sequence's own part ("Why exact attention does
 // not need a quadratic matrix", Method/Mechanism).  Every tile is kept.
 //
-// Bound: the prefix is read once for all rows, 2 B G flops a byte: HBM up to
+// Bound: the prefix is read once for all rows, B G flops a byte: HBM up to
 // about 200 rows a KV head, the tensor pipe beyond.  A 64K prefix, 8 KV heads: 47 us
 // for 4 rows a KV head (5.7 TB/s), 54 for 128; 121 for 512 (1138 TFLOP/s), where a
 // step of two tiles takes 1.97 us and its four single-CTA MMAs 1.87 of them.
