@@ -268,10 +268,10 @@ struct Scratch {
 int64_t quant_splits(const Place& p, const at::Tensor& q, const at::Tensor& k_codes, double tau) {
   const int64_t D = k_codes.size(3), tiles = (k_codes.size(1) + 127) / 128;
   const int64_t rows = std::max<int64_t>(1, k_codes.size(0) * k_codes.size(2));
-  if (!(tau > 0)) return splits_for((D == 64 ? 4 : 2) * p.sms(), rows, tiles);
+  if (!(tau > 0)) return splits_for(mala::stream_ctas(static_cast<int>(D)) * p.sms(), rows, tiles);
   // Whole waves of the CTAs that the GPU holds, of about 32 tiles a CTA: each is one KV head's, and the CTAs of a
   // row of heads drift apart over a long split (128K x 8 sequences: 337 us with 32 splits, 368 with five)
-  const int64_t slots = (D == 64 ? 4 : q.scalar_type() == at::kFloat ? 2 : 3) * static_cast<int64_t>(p.sms());
+  const int64_t slots = mala::skip_ctas(static_cast<int>(D), q.scalar_type() == at::kFloat) * static_cast<int64_t>(p.sms());
   const int64_t waves = std::max<int64_t>(1, std::llround(static_cast<double>(rows * tiles) / (32.0 * slots)));
   return std::max<int64_t>(1, std::min<int64_t>({256, tiles, slots * waves / rows}));
 }
@@ -352,7 +352,7 @@ PyObject* decode_shared(PyObject* const* a) {
                      : !sized        ? 1
                                      : mala::SharedPlan(p.sms(), static_cast<int>(B), static_cast<int>(P), static_cast<int>(N), lens != nullptr,
                                                         static_cast<int>(Hq), static_cast<int>(H)).best_splits();
-  const int64_t ss = a[10] != Py_None ? integer(a[10]) : !sized ? 1 : splits_for((D == 64 ? 4 : 2) * p.sms(), B * H, std::max<int64_t>(1, (N + 63) / 64));
+  const int64_t ss = a[10] != Py_None ? integer(a[10]) : !sized ? 1 : splits_for(mala::stream_ctas(static_cast<int>(D)) * p.sms(), B * H, std::max<int64_t>(1, (N + 63) / 64));
   const at::Tensor o = output(p, "o", a[5], {B, Hq, D}, integer(a[12]), q), lse = logs(p, a[6], {B, Hq}, integer(a[12]));
   const int b = as_int("B", B), pl = as_int("P", P), n = as_int("N", N), hq = as_int("Hq", Hq), h = as_int("Hkv", H), d = as_int("D", D);
   const int psi = as_int("prefix_splits", ps), ssi = as_int("suffix_splits", ss);

@@ -16,6 +16,7 @@
 // warp then takes the decision for itself.  The P V product of a kept tile is
 // held back by one kept tile, so that its V, loaded at the decision, lands
 // behind the next tile's scores.
+#include "shared_plan.h"
 #include "stream_common.cuh"
 
 namespace mala {
@@ -24,7 +25,7 @@ namespace {
 using namespace stream;
 
 template <int D, bool kWide>
-__global__ void __launch_bounds__(32 * kWarps, D == 64 ? 4 : kWide ? 2 : 3)
+__global__ void __launch_bounds__(32 * kWarps, skip_ctas(D, kWide))
 decode_quant_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const StreamArgs a) {
   using L = Layout<D, true>;
   constexpr int S = L::kStages, kTile = kWarps * L::kKeys;

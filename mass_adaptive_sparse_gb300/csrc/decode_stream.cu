@@ -27,6 +27,7 @@
 // never wait for one another: the last to have read a stage loads it again.
 #include <algorithm>
 
+#include "shared_plan.h"
 #include "stream_common.cuh"
 
 namespace mala {
@@ -37,7 +38,7 @@ using namespace stream;
 // CTAs an SM.  Two streams of 64 KB in flight fill the memory with 128-byte rows;
 // a third only scatters the DRAM's pages (128K x 8 sequences: 305 us with two, 341
 // with three).  Rows of 64 bytes have twice the instructions a byte.
-template <int D> constexpr int kCtas = D == 64 ? 4 : 2;
+template <int D> constexpr int kCtas = stream_ctas(D);
 
 // Keys of sequence b that count: its length, 0 if that is outside [min_len, N] (the merge reports it).
 __device__ __forceinline__ int keys_of(const StreamArgs& a, int b) {
@@ -506,7 +507,7 @@ void stream_divide(StreamArgs& a, int one_wave_on) {
   const int64_t groups = a.Hkv / a.heads_cta, units = static_cast<int64_t>(a.B) * ((a.N + a.unit - 1) / a.unit);
   int64_t z = std::min<int64_t>(static_cast<int64_t>(a.heads_cta) * a.splits * a.B, std::max<int64_t>(units, 1));
   // whole waves of CTAs, where there is more than one
-  const int64_t wave = static_cast<int64_t>(one_wave_on > 0 ? one_wave_on : sm_count()) * (a.D == 64 ? kCtas<64> : kCtas<128>);
+  const int64_t wave = static_cast<int64_t>(one_wave_on > 0 ? one_wave_on : sm_count()) * stream_ctas(a.D);
   if (z * groups > wave) z = std::max<int64_t>(1, (one_wave_on > 0 ? wave : z * groups / wave * wave) / groups);
   a.workers = static_cast<int>(z);
 }

@@ -1,5 +1,5 @@
-// How a shared decode divides the SMs between its prefix pass and its suffix pass
-// (host code; the library and the Python binding use the same).
+// How many CTAs of the decode kernels an SM holds, and how a shared decode divides the SMs between its prefix pass and its
+// suffix pass (host code; the library and the Python binding use the same).
 //
 // The prefix pass holds an SM a CTA; the suffix pass starts on the SMs it leaves
 // and goes on where its CTAs end.  The times below, in us, were fitted to device
@@ -17,6 +17,11 @@
 #include <cstdint>
 
 namespace mala {
+
+// CTAs an SM of the dense stream (decode_stream.cu) and of the skip-rule kernel (decode_quant.cu): their launch bounds,
+// and what default numbers of splits fill.  The reasons stand at the kernels.
+constexpr int stream_ctas(int D) { return D == 64 ? 4 : 2; }
+constexpr int skip_ctas(int D, bool fp32_queries) { return D == 64 ? 4 : fp32_queries ? 2 : 3; }
 
 struct SharedPlan {
   int64_t sms, batch, prefix_len, heads_kv, groups, heads_cta, rows_kv, pairs, tiles;
