@@ -349,8 +349,8 @@ size_t mala_decode_noalloc_max_floats(void);
  * A cache of K or V rows is two arrays:
  *   codes [batch, cache_len, heads_kv, head_dim]  e4m3, one byte an element
  *   exps  [batch, heads_kv, cache_len]            uint8, one byte a row, any alignment
- * The row of one (token, head) with codes c and exponent byte e stands for
- * c * 2^(e - 127).  mala_cache_write takes the smallest e >= 1 with
+ * The row of one (token, head) with codes c and exponent byte e, 1 to 254, stands
+ * for c * 2^(e - 127); e = 255 marks a row of NaN codes.  mala_cache_write takes the smallest e >= 1 with
  * max|x| <= 448 * 2^(e - 127) and rounds x * 2^(127 - e) to the nearest e4m3
  * value, ties to even.  The power-of-two scale makes this the only rounding:
  * half a step of 2^-3 relative, or 2^-10 of the scale for elements below 2^-6

@@ -8,8 +8,8 @@
 // head's group, stays below m + log l + log(tau / L).  A skipped tile loads no V.
 //
 // Bound: HBM, D + 2 bytes a key and KV head (the value's exponent comes with the
-// key's), D more in a kept tile.  8 sequences of 128K keys at tau = 1, 35
-// splits, every tile kept: 325 us, 6.7 TB/s (dense: 304).
+// key's), D more in a kept tile.  8 sequences of 128K keys at tau = 1, 28
+// splits, every tile kept: 324 us, 6.7 TB/s (dense on that machine: 314).
 //
 // One CTA of four warps per (KV head, split, sequence), a warp owns 32 keys of
 // every tile.  One barrier a tile exchanges the warps' maxima and sums; every

@@ -22,8 +22,8 @@
 // warp or more each: their rows lie side by side in memory, and one TMA box
 // brings the same keys of all of them.  (With one head a CTA, the CTAs of a row
 // drift apart and its DRAM pages are opened again for each: 5.7 TB/s with 8 KV
-// heads where 1 KV head gave 7.0.)  8 sequences of 128K keys, 32 / 8 heads: 304 us,
-// 7.1 TB/s.  The warps share the stages of the ring but
+// heads where 1 KV head gave 7.0.)  8 sequences of 128K keys, 32 / 8 heads: 304 to
+// 314 us by machine, 7.1 to 6.9 TB/s.  The warps share the stages of the ring but
 // never wait for one another: the last to have read a stage loads it again.
 #include <algorithm>
 
