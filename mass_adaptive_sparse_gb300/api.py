@@ -531,6 +531,8 @@ def cache_read(cache, T, *, dtype=None, starts=None, lens=None, out=None, stream
     k, v = (None, None) if out is None else out
     if T < 0:
         raise ValueError(f"T must not be negative, got {T}")
+    if out is not None and (k is None or v is None):
+        raise ValueError("out must be two tensors")
     code, k, v = _b().cache_read(kc, ke, vc, ve, k, v, T, -1 if dtype is None else _code(dtype), starts, lens, out is None, None)
     if code:
         _check("mala_cache_read", code)

@@ -51,3 +51,12 @@ def test_prefix_softmax_warps_stay_together_after_an_expired_wait():
     loop = role[role.index("for (int u = 0; u < steps; ++u)"):role.index("if (steps > 0)")]
     assert "tmem_ld64_sync" in loop and "mbar_arrive(smem_u32(&bars.p_ready[s]))" in loop
     assert not re.search(r"\b(break|continue|return|goto)\b", loop)
+
+
+def test_cache_read_refuses_outputs_that_are_missing():
+    """None inside `out` is not a wish for new tensors (whose rows behind the lengths nothing would write)."""
+    cache = api.quant_cache(2, 10, 2, 64, device="cpu")
+    x = torch.zeros((2, 5, 2, 64), dtype=BF16)
+    for out in ((None, x), (x, None), (None, None)):
+        with pytest.raises(ValueError, match="two tensors"):
+            api.cache_read(cache, 5, out=out)
