@@ -396,6 +396,9 @@ size_t mala_decode_quant_workspace_size(int batch, int heads_q, int head_dim, in
  * every tile is kept, and the keys are divided evenly over about num_splits
  * CTAs a sequence and KV head instead, whatever the sequences' lengths.
  *
+ * q enters the scores exactly, but for elements below 2^-24 of its row's largest
+ * (within 2^-34 of that); fp32 q with 22 bits, or within 2^-34 of its row's
+ * largest where that is more.
  * The weight p 2^e_v of a key (e_v: its value row's exponent) enters the product
  * with the codes with 11 bits (fp32 queries: 22), or within 2^-39 (2^-50) of
  * the head's largest weight where that is more.  So o is accurate element by
